@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_rows_kernel(const __grid_cons
     for (int s = 0; s < S; ++s) mbar_init(&bars[s], 1);
     fence_barrier_init();
   }
+  __syncwarp();   // the other lanes wait on these barriers: not before they exist
   const uint64_t policy = l2_policy_evict_first();
   int total = a.per;
   [[maybe_unused]] int32_t choice = -1;   // rows[lane], looked up ahead
