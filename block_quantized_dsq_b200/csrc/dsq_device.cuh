@@ -57,6 +57,10 @@ __device__ __forceinline__ float byte_value(uint32_t w) {
 // data a predecessor may have produced (and every write a predecessor may
 // still read) comes after it.  pdl_trigger() lets the next kernel launch
 // early.  Both are no-ops when the launch had no programmatic dependency.
+// Those reads are plain loads: read-only ones (__ldg, or what a const
+// __restrict__ pointer lets the compiler make of a load) are defined only for
+// data that nobody writes while the kernel runs, which begins before the wait,
+// and nothing keeps them behind it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -150,15 +150,15 @@ __device__ __forceinline__ void copy_act_to_smem(const GemvArgs &a, int64_t g0, 
   const uint4 *q = reinterpret_cast<const uint4 *>(a.xq + g0 * a.K);
   for (uint32_t g = threadIdx.x; g < nq; g += blockDim.x) {
     const uint32_t r = g / q_row, gg = g - r * q_row;   // row; word gg = 16 codes of unit gg / 16
-    reinterpret_cast<uint4 *>(sq)[r * q_row + (gg & 15u) * nunits + (gg >> 4)] = __ldg(q + g);
+    reinterpret_cast<uint4 *>(sq)[r * q_row + (gg & 15u) * nunits + (gg >> 4)] = q[g];
   }
   const uint4 *d = reinterpret_cast<const uint4 *>(a.xd + g0 * (a.K / 32));
   const uint4 *x = a.xs ? reinterpret_cast<const uint4 *>(a.xs + g0 * (a.K / 32)) : nullptr;
   for (uint32_t f = threadIdx.x; f < ns; f += blockDim.x) {
     const uint32_t r = f / s_row, ff = f - r * s_row;   // row; word ff = 4 blocks of unit ff / 2
     const uint32_t dst = r * s_row + (ff & 1u) * nunits + (ff >> 1);
-    reinterpret_cast<uint4 *>(sd)[dst] = __ldg(d + f);
-    if (x) reinterpret_cast<uint4 *>(ss)[dst] = __ldg(x + f);
+    reinterpret_cast<uint4 *>(sd)[dst] = d[f];
+    if (x) reinterpret_cast<uint4 *>(ss)[dst] = x[f];
   }
 }
 
@@ -180,7 +180,7 @@ __device__ __forceinline__ void quantize_act_to_smem(const GemvArgs &a, int64_t 
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int64_t t = base + i * blockDim.x + threadIdx.x;
-      v[i] = t < tasks ? __ldg(x4 + t) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[i] = t < tasks ? x4[t] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -456,10 +456,10 @@ __global__ void __launch_bounds__(256) gemv_q8_0_rowwise_kernel(const __grid_con
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t qw = static_cast<uint32_t>(h[1 + 2 * i]) | (static_cast<uint32_t>(h[2 + 2 * i]) << 16);
-        s = __dp4a(static_cast<int>(qw), static_cast<int>(__ldg(xq + i)), s);
+        s = __dp4a(static_cast<int>(qw), static_cast<int>(xq[i]), s);
       }
       if (ISUM) a.isum[row * nb + b] = s;
-      acc += __fmul_rn(__fmul_rn(dw, __ldg(a.xd + group * nb + b)), static_cast<float>(s));
+      acc += __fmul_rn(__fmul_rn(dw, a.xd[group * nb + b]), static_cast<float>(s));
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);

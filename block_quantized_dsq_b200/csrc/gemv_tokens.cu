@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1)
     for (uint32_t w = threadIdx.x; w < words; w += blockDim.x) {
       uint32_t v[8];
 #pragma unroll
-      for (int tok = 0; tok < 8; ++tok) v[tok] = tok < M ? __ldg(xq32 + tok * words + w) : 0u;
+      for (int tok = 0; tok < 8; ++tok) v[tok] = tok < M ? xq32[tok * words + w] : 0u;
       uint4 *dst = reinterpret_cast<uint4 *>(qt + w * 8);
       dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
       dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(kTokWarps * 32, 1)
       int32_t sm[8];
 #pragma unroll
       for (int tok = 0; tok < 8; ++tok) {
-        d[tok] = tok < M ? __ldg(a.xd + tok * nb + blk) : 0.0f;
-        sm[tok] = (TYPE == DSQ_Q4_K && tok < M) ? __ldg(a.xs + tok * nb + blk) : 0;
+        d[tok] = tok < M ? a.xd[tok * nb + blk] : 0.0f;
+        sm[tok] = (TYPE == DSQ_Q4_K && tok < M) ? a.xs[tok * nb + blk] : 0;
       }
       float4 *dd = reinterpret_cast<float4 *>(dt + blk * 8);
       dd[0] = make_float4(d[0], d[1], d[2], d[3]);

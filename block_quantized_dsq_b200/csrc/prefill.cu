@@ -1037,7 +1037,7 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
   #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const int64_t m = m0 + 32 * c + lane;
-          const int sft = (c < nchunks && m < a.M) ? __ldg(a.shift + m) : 0;
+          const int sft = (c < nchunks && m < a.M) ? a.shift[m] : 0;
           my_scale[c] = __int_as_float((127 - sft) << 23);   // s in [-113, 126]: a normal 2^-s
         }
         const bool got = wait_or_abort(s, s.accfull, static_cast<uint32_t>(i & 1), a.wait, 256);
@@ -1113,9 +1113,8 @@ __device__ __forceinline__ int row_shift(float amax) {
 // 128-byte swizzle).  BLOCKED = false writes plain row-major [M][K].  Rows
 // m >= M (padding up to whole token tiles) are written as zeros.
 template <bool BLOCKED>
-__global__ void __launch_bounds__(256) x_to_f16_kernel(const float *__restrict__ x, int64_t M, int64_t K,
-                                                       int64_t tn, __half *__restrict__ x16,
-                                                       int32_t *__restrict__ shift) {
+__global__ void __launch_bounds__(256) x_to_f16_kernel(const float *x, int64_t M, int64_t K, int64_t tn,
+                                                       __half *x16, int32_t *shift) {
   __shared__ float red[8];
   pdl_trigger();
   pdl_wait();
@@ -1139,7 +1138,7 @@ __global__ void __launch_bounds__(256) x_to_f16_kernel(const float *__restrict__
   const int64_t nv = K / 4;
   float amax = 0.0f;
   for (int64_t i = threadIdx.x; i < nv; i += blockDim.x) {
-    const float4 v = __ldg(row + i);
+    const float4 v = row[i];
     amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
   }
 #pragma unroll
@@ -1153,7 +1152,7 @@ __global__ void __launch_bounds__(256) x_to_f16_kernel(const float *__restrict__
   const float scale = __int_as_float((127 + s) << 23);
   if (threadIdx.x == 0) shift[m] = s;
   for (int64_t c = threadIdx.x; c < nchunks; c += blockDim.x) {
-    const float4 a = __ldg(row + 2 * c), b = __ldg(row + 2 * c + 1);
+    const float4 a = row[2 * c], b = row[2 * c + 1];
     const __half2 h0 = __floats2half2_rn(__fmul_rn(a.x, scale), __fmul_rn(a.y, scale));
     const __half2 h1 = __floats2half2_rn(__fmul_rn(a.z, scale), __fmul_rn(a.w, scale));
     const __half2 h2 = __floats2half2_rn(__fmul_rn(b.x, scale), __fmul_rn(b.y, scale));
@@ -1196,8 +1195,8 @@ __device__ __forceinline__ float4 sum_splits(const float4 *p, int64_t stride, in
 // Split-K partials -> output, summed in split order (deterministic).  Split
 // s's partial of the M x N outputs starts at part + s * sstride, sstride =
 // total rounded up to a multiple of 4, so every split is float4-aligned.
-__global__ void __launch_bounds__(256) splitk_reduce_kernel(const float *__restrict__ part, int64_t total,
-                                                            int64_t sstride, int splits, float *__restrict__ y) {
+__global__ void __launch_bounds__(256) splitk_reduce_kernel(const float *part, int64_t total, int64_t sstride,
+                                                            int splits, float *y) {
   pdl_trigger();
   pdl_wait();
   const int64_t n4 = total / 4, s4 = sstride / 4;
@@ -1947,14 +1946,14 @@ __global__ void __launch_bounds__(small_mma_warps(TYPE) * 32, 1)
     for (uint32_t kp = threadIdx.x; kp < kp_n; kp += blockDim.x) {
       uint32_t v[8];
 #pragma unroll
-      for (int tok = 0; tok < 8; ++tok) v[tok] = tok < M ? __ldg(x32 + tok * kp_n + kp) : 0u;
+      for (int tok = 0; tok < 8; ++tok) v[tok] = tok < M ? x32[tok * kp_n + kp] : 0u;
       const uint32_t blk32 = kp >> 4, q = kp & 15u, tq = q >> 2, c = q & 3u;   // block of 32 (unit*8 + block)
       const uint32_t slot = ((2u * blk32 + (c >> 1)) * 8u + tq + 4u * (c & 1u)) * 8u;
       uint4 *dst = reinterpret_cast<uint4 *>(xa + slot);
       dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
       dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
-    if (threadIdx.x < M) scale_back[threadIdx.x] = __int_as_float((127 - __ldg(a.shift + threadIdx.x)) << 23);
+    if (threadIdx.x < M) scale_back[threadIdx.x] = __int_as_float((127 - a.shift[threadIdx.x]) << 23);
   }
   __syncthreads();
 

@@ -16,9 +16,8 @@ namespace {
 // One 32-element block is handled by 8 consecutive lanes, 4 elements each
 // (one float4 load per lane; a warp covers 4 blocks = 512 contiguous bytes).
 
-__global__ void __launch_bounds__(256) act_q8_kernel(const float4 *__restrict__ x, int64_t nblocks,
-                                                     int8_t *__restrict__ xq, float *__restrict__ xd,
-                                                     int32_t *__restrict__ xs) {
+__global__ void __launch_bounds__(256) act_q8_kernel(const float4 *x, int64_t nblocks, int8_t *xq, float *xd,
+                                                     int32_t *xs) {
   if (threadIdx.x == 0) {
     // this CTA's slice of x toward L2 while the previous kernel finishes (a
     // hint: L2 is the point of coherence, so the predecessor's writes win)
@@ -32,7 +31,7 @@ __global__ void __launch_bounds__(256) act_q8_kernel(const float4 *__restrict__ 
   const int64_t blk = tid >> 3;
   const int sub = threadIdx.x & 7;
   const bool live = blk < nblocks;
-  const float4 v = live ? __ldg(&x[blk * 8 + sub]) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 v = live ? x[blk * 8 + sub] : make_float4(0.f, 0.f, 0.f, 0.f);
   float d;
   int s;
   const uint32_t packed = q8_block_lanes(v, d, s);

@@ -68,3 +68,19 @@ def test_barriers_exist_before_any_lane_waits(name, body):
     wait = re.search(r"mbar_wait_for|mbar_try_wait|wait_or_abort|convert_role|fused_epilogue", body)
     assert wait, name
     assert re.search(r"__syncwarp\(\)|__syncthreads\(\)|cluster_sync\(\)", body[:wait.start()]), name
+
+
+def test_read_only_loads_only_where_no_kernel_before_may_still_write():
+    """A kernel that waits for the one before (pdl_wait) runs while that one
+    writes: what it reads through the read-only path may be stale, since such a
+    load is defined only for data that nobody writes during the kernel's run and
+    may be moved above the wait.  Kernels without the wait start after it."""
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu*"))):
+        text = source(path)
+        for m in reversed(list(re.finditer(r"__global__\s+void\s+", text))):
+            start = text.index("{", matching(text, text.index("(", re.compile(r"(?:__launch_bounds__\([^)]*\))?\s*\w+").match(text, m.end()).end()), "()"))
+            end = matching(text, start)
+            if "pdl_wait" not in text[start:end]:
+                text = text[:m.start()] + text[end:]
+        left = re.findall(r"[^\n]*(?:__ldg|__restrict__|ld\.global\.nc)[^\n]*", text)
+        assert not left, (os.path.basename(path), left)
