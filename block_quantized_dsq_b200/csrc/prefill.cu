@@ -471,10 +471,12 @@ __device__ __forceinline__ Tile tile_of(const PrefillArgs &a, int64_t t) {
 // waits for a free TMEM slot, dequantizes both stages (64 elements each) into
 // its lane with two tcgen05.st, and one lane per warp arrives on the even
 // CTA's ready barrier of the slot.  The warps of J = 0 fill slots 0, 2, 4, ...
-// of the ring, those of J = 1 slots 1, 3, 5, ...
+// of the ring, those of J = 1 slots 1, 3, 5, ...  col: output column of the row
+// within the tile.  An expert's last tile runs on into the next expert's rows;
+// what those hold is not this tile's to report.
 template <int TYPE, int J, bool TAIL, int EPI, bool EXPERTS>
 __device__ __forceinline__ void convert_role(const Smem &s, const PrefillArgs &a, int64_t total, uint32_t tmem_slot0,
-                                             int rr, uint32_t ready_even) {
+                                             int rr, [[maybe_unused]] int col, uint32_t ready_even) {
   constexpr uint32_t RAW_BYTES = kRows * unit_bytes<TYPE>();
   const int lane = threadIdx.x & 31;
   const int SA = a.slots, SR = a.slots_raw;
@@ -494,7 +496,7 @@ __device__ __forceinline__ void convert_role(const Smem &s, const PrefillArgs &a
       load_pair<TYPE, J>(r, unit);
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.rempty[rs]);
-      if (!pair_in_range<TYPE, J>(r)) record_range(a.wait.status);
+      if (!pair_in_range<TYPE, J>(r) && (!EXPERTS || tl.n0 + col < a.N[0])) record_range(a.wait.status);
       if (++rs == SR) {
         rs = 0;
         rpar ^= 1u;
@@ -1012,10 +1014,11 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
     const int q = warp & 3;   // TMEM lane quadrant this warp may access
     // the raw row behind this lane: a gated unit holds 64 gate, then 64 up rows
     const int rr = EPI == kEpiGated ? 16 * q + (lane & 15) + 64 * (lane >> 4) : 32 * q + lane;
+    const int col = EPI == kEpiGated ? kRows / 2 * static_cast<int>(rank) + (rr & 63) : kRows * static_cast<int>(rank) + rr;
     const uint32_t slot0 = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + a_col0;
     const uint32_t ready_even = mapa_shared(smem_u32(s.ready), 0);
-    if (warp < kWarpConv0 + 4) convert_role<TYPE, 0, TAIL, EPI, EXPERTS>(s, a, total, slot0, rr, ready_even);
-    else convert_role<TYPE, 1, TAIL, EPI, EXPERTS>(s, a, total, slot0, rr, ready_even);
+    if (warp < kWarpConv0 + 4) convert_role<TYPE, 0, TAIL, EPI, EXPERTS>(s, a, total, slot0, rr, col, ready_even);
+    else convert_role<TYPE, 1, TAIL, EPI, EXPERTS>(s, a, total, slot0, rr, col, ready_even);
   } else {
     if constexpr (EPI == kEpiNone) {
       // ------------------------------- epilogue: TMEM -> y * 2^-s_m

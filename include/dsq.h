@@ -398,6 +398,7 @@ int dsq_moe_combine(const float *y, int64_t P, const int32_t *pos, const float *
  * unused); A: activation rows there are (a row outside them reads as zeros);
  * P: sorted rows y has room for (offsets are clamped to it); of rows, only the
  * first offsets[E] are read.  Rows of y from offsets[E] on are left as they were.  E <= 1024, E*N < 2^31, K % 256 == 0.
+ * DSQ_ERR_RANGE (dsq_gemm_experts) is recorded for blocks of experts that have sorted rows only.
  * dsq_gemv_experts: a few rows, prequantized activations (as in
  * dsq_gemv_fused), decode arithmetic.  dsq_gemm_experts: a prompt's rows, fp32
  * activations, prefill arithmetic; workspace of at least
