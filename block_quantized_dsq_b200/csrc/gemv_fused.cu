@@ -527,8 +527,7 @@ FusedKernel fused_kernel(int M, bool mma, [[maybe_unused]] int nw) {
       case 4: return gemv_fused_kernel<TYPE, 4, false, false, GATED, 8>;
       case 5: return gemv_fused_kernel<TYPE, 5, false, false, GATED, 8>;
       case 6: return gemv_fused_kernel<TYPE, 6, false, false, GATED, 8>;
-      case 7: return gemv_fused_kernel<TYPE, 7, false, false, GATED, 8>;
-      default: return gemv_fused_kernel<TYPE, 8, false, false, GATED, 8>;
+      default: return gemv_fused_kernel<TYPE, 7, false, false, GATED, 8>;   // 8 that fit take the tensor cores
     }
   }
 }

@@ -685,10 +685,9 @@ __device__ __forceinline__ void fused_epilogue(const Smem &s, const PrefillArgs 
       for (int j = 0; j < kOut; ++j)
         res[j] = (kTok * g + tok_of(j) < cnt && (col_of(j) ? live1 : live0)) ? rp[tok_of(j) * stride + col_of(j)] : 0.0f;
     };
-    if (set < ngroups) {
-      if (chains > 1) fetch_sums(set);
-      if (direct && a.residual) fetch_residual(set);
-    }
+    // (a tile is at least 32 tokens, four groups: either set has some)
+    if (chains > 1) fetch_sums(set);
+    if (direct && a.residual) fetch_residual(set);
     if (!wait_chain()) return;
     // a group's sums out of TMEM, the chains before added
     auto take = [&](int g, float (&v)[kTok]) {
@@ -759,7 +758,6 @@ __device__ __forceinline__ void fused_epilogue(const Smem &s, const PrefillArgs 
         }
       });
     }
-    if (set >= ngroups) free_chain();
     __syncwarp();   // the scales are rewritten by the next tile
   }
 }
