@@ -22,6 +22,7 @@ import hashlib
 import json
 import os
 import platform
+import re
 import statistics
 import sys
 import threading
@@ -57,11 +58,24 @@ def measured_peaks():
         return 6650.0, 1590.0, 1400.0, "fallback"
 
 
+def source_hash(name: str) -> str:
+    """Of a kernel's source file and of the headers beside it that it includes,
+    directly or through one another."""
+    csrc = os.path.join(ROOT, "block_quantized_dsq_b200", "csrc")
+    files, h = [name], hashlib.sha256()
+    for f in files:   # grows while it is walked
+        text = open(os.path.join(csrc, f), "rb").read()
+        h.update(text)
+        for inc in re.findall(rb'^#include "([^"/]+)"', text, re.M):
+            if inc.decode() not in files:
+                files.append(inc.decode())
+    return h.hexdigest()[:16]
+
+
 def traffic_record(kernel: str, workload: str):
     """dram read+write bytes per launch from the committed ncu summary, or
-    None when the kernel source changed since the counters were taken."""
-    src = os.path.join(ROOT, "block_quantized_dsq_b200", "csrc", "gemv.cu")
-    sha = hashlib.sha256(open(src, "rb").read()).hexdigest()[:16]
+    None when the kernel's sources changed since the counters were taken."""
+    sha = source_hash("gemv.cu")
     path = os.path.join(ROOT, "profiles", "traffic.txt")
     if not os.path.exists(path):
         return None

@@ -26,3 +26,22 @@ def test_reference_arm_prints_one_contract_line():
     assert d["cpu_baseline"]["cores"] >= 1
     assert d["e2e"] == {"value": d["value"], "unit": d["unit"], "h2d_bytes_per_step": 0, "d2h_bytes_per_step": 0}
     assert "paired Q8_0" in d["config"]["workload"]
+
+
+def test_traffic_record_follows_the_kernels_sources(tmp_path, monkeypatch):
+    """The recorded traffic holds for the sources it was measured on: the
+    kernel's own file and every header beside it that it includes."""
+    import shutil
+
+    import bench
+    args = ("gemv_kernel", "paired_f32_q8_0_2x8192x4096")
+    assert bench.traffic_record(*args) > bench.paired_bytes_per_call()["fused"] * 0.9
+    csrc = os.path.join("block_quantized_dsq_b200", "csrc")
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    for name in ("gemv.cu", "units.cuh", "act_q8.cuh", "dsq_host.h", "dsq_device.cuh"):
+        for part in (csrc, "profiles"):
+            shutil.copytree(os.path.join(ROOT, part), tmp_path / part, dirs_exist_ok=True)
+        assert bench.traffic_record(*args) is not None
+        with open(tmp_path / csrc / name, "a") as f:
+            f.write("\n")
+        assert bench.traffic_record(*args) is None, name
