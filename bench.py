@@ -10,7 +10,9 @@ rotated over enough copies that L2 (126 MB) cannot serve them.  The headline
 value is HBM GB/s of algorithmic bytes; the same JSON line also carries
 us/call, the roofline of the dominant kernel, an end-to-end figure through
 the public API with host buffers, the other decode workloads and the prefill
-dequant-GEMM TFLOP/s sweep, the CPU oracle baseline and clock samples.
+dequant-GEMM TFLOP/s sweep, the CPU oracle baseline and clock samples.  The
+workloads' rows are short there; all of their figures go to stderr as another
+JSON line.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl reference]
 """
@@ -468,7 +470,7 @@ def run_dsq(args, world, rank):
         "rows": rows,
         "rows_clocks": rows_clocks,
         "rows_timing": "each row: a CUDA graph of calls rotating over weight copies past 3x L2, replayed 21 "
-                       "times with CUDA events around every replay; median per call with min/max",
+                       "times with CUDA events around every replay; median per call (all figures on stderr)",
     }
     if rank == 0 and world == 1 and not args.skip_cpu:
         result["cpu_baseline"] = cpu_baseline(pairs[0], X_host, args.cpu_seconds)
@@ -907,6 +909,16 @@ def run_reference(args, world, rank):
             "e2e": {"value": round(value, 4), "unit": "GB/s", "h2d_bytes_per_step": 0, "d2h_bytes_per_step": 0}}
 
 
+def short_row(r: dict) -> dict:
+    """A row as it stands in the result line, which readers of a log's tail have
+    to get whole: its time, its rate and the fraction of the nearer peak.  All of
+    its figures go to stderr."""
+    rate = "TFLOP/s" if r.get("bound") == "tensor" else "GB/s"
+    return {"us_per_call": r["us_per_call"], rate: r[rate],
+            "frac": r.get("roofline_frac", r["hbm_frac"]),
+            **{k: r[k] for k in ("m_single_calls_us", "single_calls_us") if k in r}}
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--gpus", type=int, default=1)
@@ -941,7 +953,8 @@ def main():
             return 0
         res = run_dsq(args, world, rank)
         if rank == 0:
-            print(json.dumps(res))
+            print(json.dumps({"rows": res["rows"]}), file=sys.stderr)
+            print(json.dumps(res | {"rows": {n: short_row(r) for n, r in res["rows"].items()}}))
     finally:
         if world > 1:
             import torch.distributed as dist

@@ -45,3 +45,20 @@ def test_traffic_record_follows_the_kernels_sources(tmp_path, monkeypatch):
         with open(tmp_path / csrc / name, "a") as f:
             f.write("\n")
         assert bench.traffic_record(*args) is None, name
+
+
+def test_rows_of_the_result_line_are_short():
+    """The line is read from the end of a log: with all figures of its 56 rows it was
+    21 KB, and a reader that keeps less lost its beginning.  Rows of some 110
+    characters with their names keep it under 10."""
+    import bench
+    full = {"us_per_call": 1234.567, "median_us": 1234.567, "min_us": 1234.5, "max_us": 1299.9, "replays": 21, "calls_per_replay": 35,
+            "GB/s": 1234.5, "hbm_frac": 0.1234, "algorithmic_bytes": 123456789, "weight_copies": 35}
+    prefill = full | {"TFLOP/s": 1148.7, "bf16_peak_frac": 0.7002, "bound": "tensor", "roofline_frac": 0.7002}
+    memory = prefill | {"bound": "hbm", "roofline_frac": 0.1234}
+    assert bench.short_row(full) == {"us_per_call": 1234.567, "GB/s": 1234.5, "frac": 0.1234}
+    assert bench.short_row(prefill) == {"us_per_call": 1234.567, "TFLOP/s": 1148.7, "frac": 0.7002}
+    assert bench.short_row(memory) == {"us_per_call": 1234.567, "GB/s": 1234.5, "frac": 0.1234}
+    assert bench.short_row(full | {"m_single_calls_us": 33.28})["m_single_calls_us"] == 33.28
+    assert len(json.dumps({"prefill_grouped_q4_k_4096+1024_m2048": bench.short_row(prefill | {"single_calls_us": 119.897})})) <= 150
+    assert len(json.dumps({"prefill_q8_0_n8192_m2048": bench.short_row(prefill)})) <= 110
