@@ -53,12 +53,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int32_t 
   for (int e = threadIdx.x; e < E; e += kSortThreads) counts[blockIdx.x * static_cast<int64_t>(E) + e] = c[e];
 }
 
-// counts: [chunks][E] of the kernel before, unused when there is one chunk or the
-// CTAs are one cluster.
-template <bool CLUSTER>
+// Where the counts of all chunks come from: there is one chunk, the CTAs are one
+// cluster, or the kernel before counted (counts: [chunks][E]).
+enum : int { kSortOne = 0, kSortInCluster = 1, kSortCounted = 2 };
+template <int MODE>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t *expert, int64_t n, int64_t chunk,
                                                                   int chunks, int E, const int32_t *counts,
                                                                   int32_t *offsets, int32_t *rows, int32_t *pos) {
+  constexpr bool CLUSTER = MODE == kSortInCluster, COUNTED = MODE == kSortCounted;
   extern __shared__ int32_t table[];   // [kSortWarps][E]: first the warps' counts, then their next places
   __shared__ int32_t start[kSortMaxE + 1], scan[kSortWarps], own[CLUSTER ? kSortMaxE : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -71,9 +73,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t 
   const int64_t part = ((chunk + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
   const int64_t wlo = lo + warp * part, whi = wlo + part < hi ? wlo + part : hi;
   int32_t *mine = table + warp * E;
-  // kAhead choices of a lane are loaded at once; where that is all of them they
-  // stay in registers for the second pass (2048 x 6 choices of 64: 6.2 -> 5.3 us)
-  constexpr int kAhead = static_cast<int>(kSortChunk) / kSortThreads;
+  // kAhead choices of a lane are loaded at once, all of them up to one cluster's,
+  // and stay in registers for the second pass (2048 x 6 choices of 64: 6.2 -> 5.3
+  // us).  Beyond, a warp's many turns go faster one load at a time, and the table is
+  // read only where it is rewritten (8192 x 4 of 64: 8.4 us in the clusters' form,
+  // 7.6 so; 40,000 x 8: 26.5 and 16.3; 400,000 x 8: 75.9 and 69.1).
+  constexpr int kAhead = COUNTED ? 1 : static_cast<int>(kSortChunk) / kSortThreads;
   int ex[kAhead];
   auto load = [&](int64_t i0) {
 #pragma unroll
@@ -92,23 +97,23 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t 
   __syncthreads();
   // totals over all chunks, and over the chunks before this one (kept in before[])
   constexpr int kPer = kSortMaxE / kSortThreads;
-  int32_t total[kPer], before[kPer], held[kPer][kSortWarps];
+  int32_t total[kPer], before[kPer], held[COUNTED ? 1 : kPer][kSortWarps];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int e = static_cast<int>(threadIdx.x) * kPer + j;
     total[j] = before[j] = 0;
-    if (e >= E) continue;
+    if (e >= E || COUNTED) continue;
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) held[j][w] = table[w * E + e];
+    for (int w = 0; w < kSortWarps; ++w) held[COUNTED ? 0 : j][w] = table[w * E + e];
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) total[j] += held[j][w];
+    for (int w = 0; w < kSortWarps; ++w) total[j] += held[COUNTED ? 0 : j][w];
     if (CLUSTER) own[e] = total[j];
   }
   if constexpr (CLUSTER) cluster_sync();   // every CTA's own[] is written
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int e = static_cast<int>(threadIdx.x) * kPer + j;
-    if (e >= E || chunks == 1) continue;
+    if (e >= E || MODE == kSortOne) continue;
     total[j] = 0;
     if constexpr (CLUSTER) {
       const uint32_t at = smem_u32(&own[e]);
@@ -150,10 +155,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t 
     if (e < E) {
       start[e] = base;
       int32_t next = base + before[j];   // where this chunk's choices of e begin
+      if constexpr (COUNTED)
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) held[0][w] = table[w * E + e];
 #pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
         table[w * E + e] = next;
-        next += held[j][w];
+        next += held[COUNTED ? 0 : j][w];
       }
     }
     base += total[j];
@@ -164,7 +172,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t 
     for (int e = threadIdx.x; e <= E; e += kSortThreads) offsets[e] = start[e];
   const int64_t kept = start[E];
   for (int64_t i0 = wlo; i0 < whi; i0 += 32 * kAhead) {
-    if (whi - wlo > 32 * kAhead) load(i0);
+    if (COUNTED) load(i0);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int64_t i = i0 + j * 32 + lane;
@@ -300,7 +308,9 @@ extern "C" int dsq_moe_sort(const int32_t *expert, int64_t T, int64_t k, int64_t
     if (rc != DSQ_OK) return rc;
   }
   const size_t smem = static_cast<size_t>(kSortWarps) * E * sizeof(int32_t);
-  const auto kern = cluster ? sort_place_kernel<true> : sort_place_kernel<false>;
+  const auto kern = cluster       ? sort_place_kernel<kSortInCluster>
+                    : chunks == 1 ? sort_place_kernel<kSortOne>
+                                  : sort_place_kernel<kSortCounted>;
   rc = set_smem_once(reinterpret_cast<const void *>(kern), static_cast<int>(kSortWarps * kSortMaxE * sizeof(int32_t)),
                      "dsq_moe_sort");
   if (rc != DSQ_OK) return rc;
