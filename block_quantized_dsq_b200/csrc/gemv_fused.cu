@@ -732,9 +732,11 @@ extern "C" int dsq_gemv_experts(int type, const void *w0, const void *w1, int64_
   // One sorted row at a time streams a weight once per row, fastest while an
   // expert has about one; groups of 8 read it once for all its rows, but the
   // tensor-core form unpacks at 1.5 (Q8_0) to 3 (Q4_K) times the memory's pace.
-  // 32 experts of 4096 x 2048, even choices, one row / groups: Q8_0 28 / 34 us at
-  // 24 rows, 42 / 43 at 32, 81 / 61 at 64; Q4_K 28 / 42 at 32, 48 / 61 at 64,
-  // 87 / 68 at 128.  Uneven choices favour the groups, so Q8_0 changes over early.
+  // 32 experts of 4096 x 2048, tokens that choose 4 of them at random, one row /
+  // groups: Q8_0 30 / 36 us at 24 rows, 39 / 40 at 28, 45 / 39 at 32, 79 / 54 at 64;
+  // Q4_K 29 / 41 at 32, 49 / 60 at 64, 88 / 70 at 128.  Uneven choices (by 1 / rank)
+  // favour the groups a little sooner, 35 / 32 at 28 rows of Q8_0; rows spread
+  // evenly, a program's exception, favour single rows longer, 46 / 58 at 32.
   const bool mma = 4 * P > (type == DSQ_Q8_0 ? 3 : 8) * E && 8 * act_bytes_per_token(type, K) <= kTokMaxActSmem;
   cudaStream_t st = as_stream(stream);
   if (!mma && rows_fit(K, N, P)) {

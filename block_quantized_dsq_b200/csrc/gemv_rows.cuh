@@ -302,7 +302,8 @@ int rows_launch(const char *name, int type, RowsArgs &a, bool gated, bool expert
   const int64_t rows = groups * a.N * (gated ? 2 : 1);
   const bool mid = rows >= kRowsMid * static_cast<int64_t>(sms) && rows < kRowsLong * static_cast<int64_t>(sms);
   const int nw = type == DSQ_Q4_K && mid ? 12 : 8;
-  // two slots a warp, four where a slot is small: about 140 KB in flight an SM
+  // 8 warps: two slots each, about 140 KB in flight an SM, or four small ones; 12
+  // warps: one, 110 KB; one too for Q8_0 pairs of the longest rows
   const size_t per_stage = static_cast<size_t>(nw) * a.slot_bytes;
   a.stages = per_stage <= 40 * 1024 ? 4 : per_stage <= 80 * 1024 ? 2 : 1;
   const size_t smem = per_stage * a.stages + nw * a.stages * sizeof(uint64_t);

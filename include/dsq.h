@@ -305,8 +305,9 @@ typedef enum dsq_gate {
  * Mean squares are held in 64 bits and r is rounded to fp32 once; every other
  * step is one fp32 operation in the order written.  A call repeats bit for bit;
  * another M may take another launch shape, whose r is the same but where the
- * 64-bit value lies at the middle of two fp32 numbers (about one row in 10^8).  h_out may be h or b, and x may be b
- * (each element is read before it is written); no other overlap.
+ * 64-bit value lies at the middle of two fp32 numbers (about one row in 10^8).
+ * h_out may be h or b, and x may be b (each element is read before it is
+ * written); no other overlap.
  * 1 <= K <= 32768, any M; all pointers 16-byte aligned.
  */
 int dsq_norm_block(const float *h, const float *b, const float *w_post, int gate_kind,
@@ -353,8 +354,8 @@ int dsq_gemv_fused(int type, const void *w0, const void *w1, int64_t N, int64_t 
  * epilogue's own, so the sums agree with dsq_gemm_prefill's in rounding only,
  * not bit for bit.  workspace: at least
  * dsq_prefill_fused_workspace_bytes(type, w1 != NULL, N, K, M) bytes, 256-byte
- * aligned.  Requires K % 256 == 0, 1 <= M, N >= 1; x, w0, w1, y and residual
- * 16-byte aligned.
+ * aligned.  Requires K % 256 == 0, 1 <= M, N >= 1 (a pair's N <= 2^23 where up
+ * to 8 tokens take the small kernels); x, w0, w1, y and residual 16-byte aligned.
  */
 int dsq_gemm_prefill_fused(int type, const void *w0, const void *w1, int64_t N, int64_t K,
                            const float *x, int64_t M, int act, const float *bias0,
@@ -370,7 +371,8 @@ size_t dsq_prefill_fused_workspace_bytes(int type, int gated, int64_t N, int64_t
  * t*k + j at each sorted row (-1 at rows >= offsets[E]); pos [T][k], the
  * sorted row of each choice (-1 where it was dropped).  Choices of one expert
  * keep their order.  workspace: dsq_moe_sort_workspace_bytes(T, k, E) bytes
- * (0 for small calls: it may then be NULL), 256-byte aligned.
+ * (0 up to 2048 choices: it may then be NULL), 256-byte aligned; only calls of
+ * more than 16,384 choices write to it.
  * E <= 1024, T*k <= 2^30; T == 0 gives all-zero offsets.
  */
 int dsq_moe_sort(const int32_t *expert, int64_t T, int64_t k, int64_t E, int32_t *offsets,
@@ -384,6 +386,7 @@ size_t dsq_moe_sort_workspace_bytes(int64_t T, int64_t k, int64_t E);
  * j in order, fp32.  y [P][N]; a pos outside [0, P) adds nothing, whatever its
  * weight.  weight [T][k] may be NULL (1), residual [T][N] may be NULL (0) and
  * may be out.  T == 0 is a no-op.  y, residual and out 16-byte aligned.
+ * k <= 1024, T and P < 2^31, N <= 2^24 (<= 65535 * 128 where N % 4 != 0).
  */
 int dsq_moe_combine(const float *y, int64_t P, const int32_t *pos, const float *weight,
                     const float *residual, int64_t T, int64_t k, int64_t N, float *out,
@@ -397,13 +400,20 @@ int dsq_moe_combine(const float *y, int64_t P, const int32_t *pos, const float *
  * a_p is activation row rows[p] / k, or row p when rows is NULL (k is then
  * unused); A: activation rows there are (a row outside them reads as zeros);
  * P: sorted rows y has room for (offsets are clamped to it); of rows, only the
- * first offsets[E] are read.  Rows of y from offsets[E] on are left as they were.  E <= 1024, E*N < 2^31, K % 256 == 0.
- * DSQ_ERR_RANGE (dsq_gemm_experts) is recorded for blocks of experts that have sorted rows only.
+ * first offsets[E] are read.  Rows of y from offsets[E] on are left as they
+ * were.  E <= 1024, E*N < 2^31 - 256, K % 256 == 0.
  * dsq_gemv_experts: a few rows, prequantized activations (as in
- * dsq_gemv_fused), decode arithmetic.  dsq_gemm_experts: a prompt's rows, fp32
- * activations, prefill arithmetic; workspace of at least
- * dsq_experts_workspace_bytes(type, w1 != NULL, E, N, K, P) bytes, 256-byte
- * aligned.  P == 0 or N == 0 is a no-op.
+ * dsq_gemv_fused), decode arithmetic.  K + K/8 (+ K/8 for Q4_K) <= 65536; P, A
+ * and k <= 2^30.  P / E also chooses the kernel (the device alone knows how many
+ * rows there are): above 3/4 (Q8_0) or 2 (Q4_K) an expert's weights are read once
+ * for up to 8 of its rows, else once a row.  Above K = 7168 (Q8_0) or 6400 (Q4_K)
+ * 8 rows' activations do not fit and every row reads them: many rows of such
+ * a K are dsq_gemm_experts' to take.
+ * dsq_gemm_experts: a prompt's rows, fp32 activations, prefill arithmetic;
+ * workspace of at least dsq_experts_workspace_bytes(type, w1 != NULL, E, N, K,
+ * P) bytes, 256-byte aligned.  K <= 65536; N, P, A and k <= 2^24.  DSQ_ERR_RANGE
+ * is recorded for blocks of experts that have sorted rows only.
+ * P == 0 or N == 0 is a no-op.
  */
 int dsq_gemv_experts(int type, const void *w0, const void *w1, int64_t E, int64_t N, int64_t K,
                      const int32_t *offsets, const int32_t *rows, int64_t k, int64_t P,
